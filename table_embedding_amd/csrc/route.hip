@@ -189,7 +189,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, bool vec) 
       const int j = jb * L + lane;
       if (j < a.k) {
         a.ids[t * a.k + j] = (int32_t)id_mine[jb];
-        a.weights[t * a.k + j] = x_mine[jb] * inv;
+        // (a choice that is not there weighs 0 also where inv is NaN)
+        a.weights[t * a.k + j] = id_mine[jb] == 0xffffffffu ? 0.f : x_mine[jb] * inv;
       }
     }
   }
