@@ -365,6 +365,8 @@ class F8Matrix:
         vs, ss = self.shapes(rows, cols, square, tuple(values.shape[:-2]))
         if not values.is_cuda or not scales.is_cuda:
             raise ValueError("values and scales must be device tensors")
+        if values.get_device() != scales.get_device():
+            raise ValueError("values and scales must be on one device")
         _whole(values, "values", (_F8,), vs)
         _whole(scales, "scales", (torch.uint8,), ss)
         self.values, self.scales = values, scales
@@ -470,7 +472,7 @@ def tbe_matmul_f8(a: F8Matrix, b: F8Matrix, offsets: Optional[torch.Tensor], out
     o, ldo = _matrix(out, "out", (out.dtype,))
     if out.shape != (a.rows, b.rows):
         raise ValueError(f"out must be [{a.rows}, {b.rows}]")
-    st = _on(stream, a.values, b.values, offsets, out)
+    st = _on(stream, a.values, a.scales, b.values, b.scales, offsets, out)
     if offsets is None and experts != 1:
         raise ValueError("several experts need offsets")
     _check("tbe_matmul_f8", lib().tbe_matmul_f8(
@@ -497,7 +499,7 @@ def tbe_matmul_f8_segments(a: F8Matrix, b: F8Matrix, offsets: torch.Tensor, out:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     dt = _out_type(out.dtype)
     experts = _width(offsets, "offsets", 1) - 1
-    st = _on(stream, a.values, b.values, offsets, out)
+    st = _on(stream, a.values, a.scales, b.values, b.scales, offsets, out)
     _check("tbe_matmul_f8_segments", lib().tbe_matmul_f8_segments(
         experts, a.rows, b.rows, a.cols, a.values.data_ptr(), a.scales.data_ptr(),
         b.values.data_ptr(), b.scales.data_ptr(),
