@@ -46,7 +46,7 @@ __device__ __forceinline__ void find_tile(const int32_t* start, int32_t E, int b
   for (int32_t e0 = 0; e0 <= E + 1; e0 += kWave) {
     const int32_t q = e0 + lane;
     const int32_t lo = q <= E + 1 ? start[q] : 0, up = q <= E + 1 ? start[q + 1] : 0;
-    const int32_t t = up > lo ? (up - lo + bm - 1) / bm : 0;
+    const int32_t t = up > lo ? (up - lo - 1) / bm + 1 : 0;  // up - lo may be all of 31 bits
     int32_t x = t;
 #pragma unroll
     for (int m = 1; m < kWave; m <<= 1) {

@@ -28,3 +28,17 @@ def test_route_absent_choices_weigh_zero_beside_nan_and_inf(e, dtype):
         want_ids, want_w = R.route(x.double().numpy(), 5, None, renorm)
         assert np.array_equal(ids.cpu().numpy(), want_ids)
         assert np.array_equal(R.f64(w), want_w, equal_nan=True)
+
+
+# ------------------------------------------------------------------ 8-bit product
+
+
+def test_product_of_a_segment_of_almost_2_to_31_rows():
+    """Its row tiles are counted without passing 32 bits (without a contraction: the
+    operands take no memory, the results are zeros)."""
+    m = (1 << 31) - 2
+    a, b = te().quantize_f8(torch.empty(m, 0).cuda()), te().quantize_f8(torch.empty(1, 0).cuda())
+    offsets = torch.tensor([0, m], dtype=torch.int32).cuda()
+    y = torch.full((m, 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    te().tbe_matmul_f8(a, b, offsets, y)
+    assert not y.any()
