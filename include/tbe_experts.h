@@ -115,7 +115,8 @@ int tbe_expert_combine_backward(int64_t tokens, int32_t k, int64_t rows, int64_t
  * The 8-bit form of a matrix [R, C] with blocks along C: values e4m3 [R, Cp],
  * Cp = C rounded up to 128 (zeros beyond C), and one scale byte s per block of
  * 128 columns, [R, Sp], Sp = Cp / 128 rounded up to 4: a value stands for
- * value * 2^(s - 127).  The exponent s - 127 is the smallest e >= -126 with
+ * value * 2^(s - 127), and every value of a block with s = 255 for NaN
+ * (tbe_quantize_f8 writes 1 to 247).  The exponent s - 127 is the smallest e >= -126 with
  * max|x| / 448 <= 2^e over the block's finite elements, so the largest one
  * keeps its place in e4m3's range and scaling is exact; rounding is to the
  * nearest, ties to even; infinities and NaN become NaN.  Bytes of a scale row

@@ -356,7 +356,7 @@ class F8Matrix:
     """A matrix [rows, cols], or one for each expert, in the 8-bit form: values
     e4m3 [..., rows, cols rounded up to 128], scales uint8 [..., rows or (square)
     ceil(rows / 128), blocks of 128 columns rounded up to 4].  A value stands for
-    value * 2^(scale - 127)."""
+    value * 2^(scale - 127), or NaN at a scale of 255."""
 
     __slots__ = ("values", "scales", "rows", "cols", "square")
 
@@ -396,7 +396,10 @@ class F8Matrix:
         e = e.repeat_interleave(TBE_F8_BLOCK, dim=-1)
         if self.square:
             e = e.repeat_interleave(TBE_F8_BLOCK, dim=-2)[..., :self.rows, :]
-        by = (e << 23).view(torch.float32)
+        # the byte is float32's exponent field, but for its ends: 2^-127 is subnormal there, and
+        # 255 is no number
+        by = (e << 23).masked_fill(e == 0, 1 << 22).masked_fill(e == 255, 0x7fc00000)
+        by = by.view(torch.float32)
         return (self.values.float() * by)[..., :self.cols]
 
 

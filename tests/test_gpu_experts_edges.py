@@ -42,3 +42,29 @@ def test_product_of_a_segment_of_almost_2_to_31_rows():
     y = torch.full((m, 1), 7.0, dtype=torch.bfloat16, device="cuda")
     te().tbe_matmul_f8(a, b, offsets, y)
     assert not y.any()
+
+
+@pytest.mark.parametrize("square", [False, True])
+def test_every_scale_byte_stands_for_the_same_in_checks_and_products(square):
+    """F8Matrix.float() and the product agree on all 256 bytes: 2^(s - 127), NaN for 255."""
+    rows = 256 * (128 if square else 1)
+    values = torch.full((rows, 128), 448.0).to(torch.float8_e4m3fn).cuda()
+    values[:, 1::2] = 0
+    scales = torch.zeros(256, 4, dtype=torch.uint8)
+    scales[:, 0] = torch.arange(256)
+    a = te().F8Matrix(values, scales.cuda(), rows, 128, square)
+    want = 448.0 * np.exp2(np.arange(256) - 127.0)
+    got = R.f64(a.float())[::128 if square else 1]
+    assert np.isnan(got[255]).all() and not np.isnan(got[:255]).any()
+    # 448 * 2^(s - 127) passes float32 from s = 247 on
+    assert np.array_equal(got[:247, 0], want[:247]) and np.isinf(got[247:255, 0]).all()
+    assert not got[:255, 1].any()
+    # against 64 elements of 2^-6 at the scale that brings the sum to 448 * 2^-3
+    one = torch.full((1, 128), 2.0 ** -6).to(torch.float8_e4m3fn).cuda()
+    for s in (0, 1, 2, 100, 127, 200, 247, 253, 254):
+        by = torch.zeros(1, 4, dtype=torch.uint8)
+        by[0, 0] = 254 - s - 3 if s < 252 else 0
+        b = te().F8Matrix(one, by.cuda(), 1, 128)
+        y = R.f64(te().matmul_f8(b, a))[0, ::128 if square else 1]
+        assert y[s] == 448 * 2.0 ** (s - 127 + int(by[0, 0]) - 127)
+        assert np.isnan(y[255])
