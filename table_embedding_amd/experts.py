@@ -88,6 +88,13 @@ def _on(stream, first, *tensors):
 _I32, _F32 = (torch.int32,), (torch.float32,)
 
 
+def _counts(*counts):
+    """Counts that the library takes in 32 bits (its binding would drop the bits above)."""
+    for n in counts:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"a count of {n} does not fit 32 bits")
+
+
 def _width(t, name, dims=2):
     """Size of the last of a tensor's `dims` dimensions."""
     if not isinstance(t, torch.Tensor):
@@ -104,6 +111,7 @@ def tbe_route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor], flags
               ids: torch.Tensor, weights: torch.Tensor, stream=None) -> None:
     p, ld = _matrix(logits, "logits")
     n, e = logits.shape
+    _counts(k, e)
     st = _on(stream, logits, valid, ids, weights)
     v = None
     if valid is not None:
@@ -119,6 +127,7 @@ def tbe_route_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights: to
     (p, ld), (g, ldg) = _matrix(logits, "logits"), _matrix(grad_logits, "grad_logits")
     n, e = logits.shape
     k = _width(ids, "ids")
+    _counts(k, e)
     if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype:
         raise ValueError("grad_logits must have the logits' shape and dtype")
     st = _on(stream, logits, ids, grad_weights, grad_logits)
@@ -135,6 +144,7 @@ def route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = None,
     (`renormalize`).  valid: uint8 or bool [N], tokens with 0 get no expert."""
     p, ld = _matrix(logits, "logits")
     n, e = logits.shape
+    _counts(k, e)
     st = _on(None, logits, valid)
     v = None
     if valid is not None:
@@ -154,6 +164,7 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights: torch.
     p, ld = _matrix(logits, "logits")
     n, e = logits.shape
     shape = (n, _width(ids, "ids"))
+    _counts(shape[1], e)
     st = _on(None, logits, ids, grad_weights)
     i, w = _whole(ids, "ids", _I32, shape), _whole(grad_weights, "grad_weights", _F32, shape)
     grad = torch.empty_like(logits, memory_format=torch.contiguous_format)
@@ -168,6 +179,7 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights: torch.
 
 @functools.lru_cache(maxsize=256)  # a function of its sizes alone
 def tbe_expert_rows(tokens: int, k: int, experts: int, align: int) -> int:
+    _counts(k, experts, align)
     n = C.c_int64()
     _check("tbe_expert_rows", lib().tbe_expert_rows(tokens, k, experts, align, C.byref(n)))
     return n.value
@@ -175,6 +187,7 @@ def tbe_expert_rows(tokens: int, k: int, experts: int, align: int) -> int:
 
 @functools.lru_cache(maxsize=256)
 def tbe_expert_sort_workspace_size(tokens: int, k: int, experts: int, align: int) -> int:
+    _counts(k, experts, align)
     n = C.c_size_t()
     _check("tbe_expert_sort_workspace_size",
            lib().tbe_expert_sort_workspace_size(tokens, k, experts, align, C.byref(n)))
@@ -204,8 +217,9 @@ def tbe_expert_dispatch(x: torch.Tensor, slots: torch.Tensor, source: torch.Tens
     rows = out.shape[0]
     if out.shape[1] != w:
         raise ValueError("x and out must have one width")
-    st = _on(stream, x, slots, source, out)
     k = _width(slots, "slots")
+    _counts(k)
+    st = _on(stream, x, slots, source, out)
     _check("tbe_expert_dispatch", lib().tbe_expert_dispatch(
         n, k, rows, w, WDTYPE_OF_TORCH[x.dtype], p, ldx, _whole(slots, "slots", _I32, (n, k)),
         _whole(source, "source", _I32, (rows,)), o, ldo, st))
@@ -216,6 +230,7 @@ def tbe_expert_dispatch_f8(x: torch.Tensor, slots: torch.Tensor, source: torch.T
     p, ldx = _matrix(x, "x")
     n, w = x.shape
     rows, k = _width(source, "source", 1), _width(slots, "slots")
+    _counts(k)
     st = _on(stream, x, slots, source, values, scales)
     vs, ss = F8Matrix.shapes(rows, w)
     _check("tbe_expert_dispatch_f8", lib().tbe_expert_dispatch_f8(
@@ -229,6 +244,7 @@ def tbe_expert_combine(y: torch.Tensor, slots: torch.Tensor, weights: Optional[t
     (p, ldy), (o, ldo) = _matrix(y, "y"), _matrix(out, "out", (y.dtype,))
     rows, w = y.shape
     n, k = out.shape[0], _width(slots, "slots")
+    _counts(k)
     if out.shape[1] != w:
         raise ValueError("y and out must have one width")
     st = _on(stream, y, slots, weights, out)
@@ -247,6 +263,7 @@ def tbe_expert_combine_backward(grad_out: torch.Tensor, y: torch.Tensor, slots: 
     (p, ldy), (o, ldo) = _matrix(y, "y", same), _matrix(grad_y, "grad_y", same)
     rows, w = y.shape
     n, k = grad_out.shape[0], _width(slots, "slots")
+    _counts(k)
     if grad_out.shape[1] != w or grad_y.shape != y.shape:
         raise ValueError("grad_out, y and grad_y must have one width, grad_y the rows of y")
     st = _on(stream, grad_out, y, slots, source, weights, grad_y, grad_weights)
@@ -467,6 +484,7 @@ def _out_type(dtype):
 def tbe_matmul_f8(a: F8Matrix, b: F8Matrix, offsets: Optional[torch.Tensor], out: torch.Tensor,
                   stream=None) -> None:
     experts = b.values.shape[0] if b.values.dim() == 3 else 1
+    _counts(experts)
     if a.values.dim() != 2 or a.square or b.values.dim() > 3:
         raise ValueError("a must be one matrix with a scale a row, b one or one an expert")
     if a.cols != b.cols:
@@ -502,6 +520,7 @@ def tbe_matmul_f8_segments(a: F8Matrix, b: F8Matrix, offsets: torch.Tensor, out:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     dt = _out_type(out.dtype)
     experts = _width(offsets, "offsets", 1) - 1
+    _counts(experts)
     st = _on(stream, a.values, a.scales, b.values, b.scales, offsets, out)
     _check("tbe_matmul_f8_segments", lib().tbe_matmul_f8_segments(
         experts, a.rows, b.rows, a.cols, a.values.data_ptr(), a.scales.data_ptr(),

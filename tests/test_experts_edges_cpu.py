@@ -72,3 +72,40 @@ def test_products_look_at_the_devices_of_scales(which):
     with pytest.raises(ValueError, match="one device"):
         te.tbe_matmul_f8_segments(a, b, offsets,
                                   _On.on(torch.zeros(1, 4, 8, dtype=torch.bfloat16), 0))
+
+
+@pytest.mark.parametrize("big", [(1 << 32) + 2, -(1 << 32) + 2, 1 << 31])
+def test_counts_past_32_bits_are_refused(big):
+    """Counts travel to the library in 32 bits: none is taken modulo 2^32."""
+    x, ids = torch.zeros(0, 4), torch.zeros(0, 2, dtype=torch.int32)
+    for call in (lambda: te.tbe_expert_rows(4, big, 8, 1), lambda: te.tbe_expert_rows(4, 2, big, 1),
+                 lambda: te.tbe_expert_rows(4, 2, 8, big),
+                 lambda: te.tbe_expert_sort_workspace_size(4, big, 8, 1),
+                 lambda: te.tbe_expert_sort_workspace_size(4, 2, big, 1),
+                 lambda: te.tbe_expert_sort_workspace_size(4, 2, 8, big),
+                 lambda: te.ExpertRows(ids, big), lambda: te.ExpertRows(ids, 4, align=big),
+                 lambda: te.tbe_route(x, big, None, 0, ids, torch.zeros(0, 2)),
+                 lambda: te.route(x, big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    if big > 0:  # experts that a row is wide: a view of one element
+        wide = torch.empty(1).expand(0, big)
+        some = torch.zeros(0, 2)
+        for call in (lambda: te.route(wide, 2), lambda: te.route_backward(wide, ids, some),
+                     lambda: te.tbe_route(wide, 2, None, 0, ids, some),
+                     lambda: te.tbe_route_backward(wide, ids, some, 0, wide)):
+            with pytest.raises(ValueError, match="32 bits"):
+                call()
+        slots, row = torch.empty(1, dtype=torch.int32).expand(0, big), torch.zeros(0, 8)
+        source, f8 = torch.zeros(0, dtype=torch.int32), _f8(4, 128, 0, 0)
+        many = torch.empty(1, dtype=torch.int32).expand(big + 1)
+        each = _f8(4, 128, 0, 0)
+        each.values = each.values.as_subclass(torch.Tensor)[None].expand(big, 4, 128)
+        for call in (lambda: te.tbe_expert_dispatch(row, slots, source, row),
+                     lambda: te.tbe_expert_dispatch_f8(row, slots, source, row, row),
+                     lambda: te.tbe_expert_combine(row, slots, None, row),
+                     lambda: te.tbe_expert_combine_backward(row, row, slots, source, row, row, row),
+                     lambda: te.tbe_matmul_f8(f8, each, many, row),
+                     lambda: te.tbe_matmul_f8_segments(f8, f8, many, row.bfloat16())):
+            with pytest.raises(ValueError, match="32 bits"):
+                call()
