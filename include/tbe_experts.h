@@ -171,12 +171,15 @@ int tbe_matmul_f8_segments(int32_t experts, int64_t p, int64_t q, int64_t rows,
  *
  * norm = sqrt(sum over all tensors of x^2); outs[i] = grads[i] * min(1,
  * max_norm / (norm + 1e-6)), computed in float32 and rounded to the tensor's
- * type.  grads, outs, sizes and dtypes are host arrays of n entries (n may be
- * any number, sizes may be 0); outs null, or an entry equal to its gradient:
+ * type.  grads, outs, sizes and dtypes are host arrays of n entries (n may be 0
+ * to 2^20, TBE_E_UNSUPPORTED beyond; a size 0 to 2^36, TBE_E_RANGE beyond); outs
+ * null, or an entry equal to its gradient:
  * in place, where a factor of 1 writes nothing.  A NaN norm gives NaN
  * everywhere, an infinite one a factor of 0, as the formula has it.  Squares
  * are added in float64 in a fixed order: repeated calls give the same bits.
- * norm: device float32, one value. */
+ * norm: device float32, one value.  Other errors: TBE_E_ARG (null or misaligned
+ * pointers, negative sizes, unknown dtype, max_norm negative or NaN),
+ * TBE_E_WORKSPACE (ws too small or not 256-byte aligned). */
 int tbe_clip_workspace_size(int32_t n, const int64_t* sizes, size_t* bytes);
 int tbe_clip_grad_norm(int32_t n, const void* const* grads, void* const* outs,
                        const int64_t* sizes, const int32_t* dtypes, float max_norm, float* norm,

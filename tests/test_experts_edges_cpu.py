@@ -109,3 +109,13 @@ def test_counts_past_32_bits_are_refused(big):
                      lambda: te.tbe_matmul_f8_segments(f8, f8, many, row.bfloat16())):
             with pytest.raises(ValueError, match="32 bits"):
                 call()
+
+
+def test_clip_limits_are_those_of_the_header():
+    import ctypes as C
+    n, size = (1 << 20) + 1, C.c_size_t()
+    f = te.lib().tbe_clip_workspace_size
+    assert f(n, (C.c_int64 * n)(), C.byref(size)) == te.TBE_E_UNSUPPORTED
+    assert f(n - 1, (C.c_int64 * n)(), C.byref(size)) == te.TBE_OK
+    assert f(1, (C.c_int64 * 1)((1 << 36) + 1), C.byref(size)) == te.TBE_E_RANGE
+    assert f(1, (C.c_int64 * 1)(1 << 36), C.byref(size)) == te.TBE_OK
