@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from tests import experts_ref as R
-from tests.test_gpu_experts import TYPES, te
+from tests.test_gpu_experts import (HALF_ULP, TINY, TYPES, check_form, close, hard_matrix, rnd,
+                                    strided, te)
 
 pytestmark = pytest.mark.gpu
 
@@ -137,3 +138,87 @@ def test_product_over_four_million_columns(kind):
         return (torch.rand(rows, k, generator=g, device="cuda") + 0.5).to(torch.bfloat16)
     a, b = te().quantize_f8(values(32, 1.125)), te().quantize_f8(values(24, 1.125))
     check_sums(te().matmul_f8(a, b), a.float(), b.float(), k, 2.0 ** -8)
+
+
+def bad_places(x, spread):
+    """x with infinities and NaN at even and odd columns and rows, at the ends of blocks,
+    beside the largest finite value, and a block of nothing else."""
+    inf, nan = float("inf"), float("nan")
+    r, c = x.shape
+    for i, (row, col, v) in enumerate([(0, 0, inf), (0, 3, -inf), (1, 126, nan), (1, 128, inf),
+                                       (2, 127, -nan), (2, 200, inf), (r - 1, c - 1, nan),
+                                       (r - 1, c - 2, -inf), (r // 2, 64, inf), (r // 2, 65, nan)]):
+        if row < r and col < c and (spread or i % 2):
+            x[row, col] = v
+    if r > 5 and c > 128:
+        x[4, :128] = inf
+        x[5, :128:2], x[5, 1:128:2] = nan, -inf
+        x[3, 130 % c] = torch.finfo(x.dtype).max
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("r,c,pad", [(9, 256, 0), (130, 259, 0), (257, 136, 1), (6, 130, 8)])
+def test_quantize_not_finite(r, c, pad, spread, dtype):
+    """Infinities and NaN become NaN in every form and type, and leave the scales to the
+    finite elements beside them."""
+    x = bad_places(hard_matrix(r, c, dtype, 3), spread)
+    h = R.f64(x)
+    x = strided(x, pad) if pad else x
+    for square in (False, True):
+        check_form(te().quantize_f8(x, square=square), h, square, "rows")
+        check_form(te().quantize_f8(x, transpose=True, square=square), h.T, square, "columns")
+        a, b = te().quantize_f8_pair(x, square=square)
+        check_form(a, h, square, "pair rows")
+        check_form(b, h.T, square, "pair columns")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("n,width", [(9, 256), (130, 259), (6, 1030)])
+def test_dispatch_f8_not_finite(n, width, dtype):
+    g = np.random.default_rng([n, width])
+    ids = g.integers(-1, 5, size=(n, 3))
+    r = te().ExpertRows(torch.from_numpy(ids).int().cuda(), 5, align=16)
+    x = bad_places(hard_matrix(n, width, dtype, 4), True)
+    rows = R.f64(r.dispatch(x))
+    check_form(r.dispatch_f8(x), rows, False, "dispatched")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("e", [7, 64, 65, 128, 129, 256, 300, 512, 513, 1024])
+def test_route_gradient_of_every_layout_by_probability(e, dtype):
+    """Each element of the gradient within its own softmax term's bound."""
+    k = min(e, 9)
+    g = np.random.default_rng([e, 2])
+    x = torch.from_numpy(g.integers(-40, 41, size=(11, e)) / 8.0).to(TYPES[dtype]).cuda()
+    x[3, ::3] = -float("inf")
+    for renorm in (False, True):
+        ids, _ = te().route(x, k, renormalize=renorm)
+        dw = rnd(11, k, seed=e)
+        h, pick = R.f64(x), ids.cpu().numpy().astype(np.int64)
+        want = R.route_backward(h, pick, R.f64(dw), renorm)
+        p = np.exp(h - h.max(axis=1, keepdims=True))
+        chosen = np.zeros_like(p)
+        np.put_along_axis(chosen, np.where(pick < 0, 0, pick), 1.0, 1)
+        p = p * chosen if renorm else p
+        p /= p.sum(axis=1, keepdims=True)
+        # p and the dot product carry the softmax's (e + 8) roundings each, and the
+        # difference of two terms of at most max|dw| its own
+        scale = 2 * np.abs(R.f64(dw)).max(axis=1, keepdims=True)
+        close(te().route_backward(x, ids, dw, renormalize=renorm), want,
+              (2 * e + 16) * 2.0 ** -24 * scale * p + HALF_ULP[dtype] * np.abs(want)
+              + TINY[dtype], "grad_logits")
+
+
+def test_products_repeat_themselves():
+    """The same bits from the same operands, whatever the tile."""
+    for rows, n, k in ((300, 200, 1000), (2300, 2100, 520), (6500, 2304, 512)):
+        a, b = te().quantize_f8(rnd(rows, k, dtype="bf16")), te().quantize_f8(rnd(n, k, seed=2))
+        first = te().matmul_f8(a, b)
+        assert all(torch.equal(te().matmul_f8(a, b), first) for _ in range(4)), (rows, n, k)
+        ends = torch.tensor([0, 128, 512], dtype=torch.int32).cuda()
+        at = te().quantize_f8(rnd(512, rows, dtype="bf16"), transpose=True)
+        bt = te().quantize_f8(rnd(512, n, dtype="bf16", seed=3), transpose=True)
+        one = te().matmul_f8_segments(at, bt, ends)
+        assert all(torch.equal(te().matmul_f8_segments(at, bt, ends), one) for _ in range(4))
