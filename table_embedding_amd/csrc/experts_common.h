@@ -120,10 +120,6 @@ __device__ __forceinline__ void st_elem(void* p, int64_t e, float v) {
 // VEC consecutive elements (VEC = 1, or the 16 bytes of the type).
 template <int WD> constexpr int kVec16 = WD == WD_F32 ? 4 : 8;
 template <int WD, int VEC>
-__device__ __forceinline__ void ld_vec(const void* p, int64_t e, float* v) {
-  if constexpr (VEC == 1) v[0] = ld_elem<WD>(p, e); else load_w<WD, VEC>(p, e, v);
-}
-template <int WD, int VEC>
 __device__ __forceinline__ void st_vec(void* p, int64_t e, const float* v) {
   if constexpr (VEC == 1) st_elem<WD>(p, e, v[0]); else store_w<WD, VEC>(p, e, v);
 }
