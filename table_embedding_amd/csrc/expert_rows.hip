@@ -4,9 +4,9 @@
 // counts, an exclusive prefix of each expert's counts over the tiles, then the
 // placement, where a choice's rank inside its tile is the number of equal ids
 // before it.  Everything that follows is row traffic, bound by memory: each
-// kernel walks the tokens, so a token's row crosses memory once however many
-// experts take it, and the rows that hold no choice are zeroed by workgroups
-// of the same launch.
+// kernel walks the tokens, so a token's row is read once however many experts
+// take it (the combination's gradient reads it once for every four choices), and
+// the rows that hold no choice are zeroed by workgroups of the same launch.
 //
 // Measured with 32768 tokens of 2048 bfloat16 columns, 4 choices of 64 experts,
 // segments aligned to 128 (139264 rows):
@@ -202,7 +202,12 @@ __global__ __launch_bounds__(kThreads) void expert_place_kernel(ExpertSortArgs a
 // The whole sort in one workgroup of 1024 threads, for batches of at most
 // kSortOneIds choices and kSortOneRows rows: a wave takes ROUNDS consecutive
 // rounds of 64 ids, all loaded at once; counts and placements stay in LDS, one
-// launch.  (6002 choices of 24 experts: three launches 18 us, this one 9 us.)
+// launch.  The limit, us on the device by one launch / by three:
+//   choices       1024          4096          8192
+//   24 experts    4.9 / 15.4    6.0 / 15.0    9.3 / 14.9
+//   256           6.8 / 16.4    8.8 / 16.0   13.1 / 15.7
+//   1024         11.7 / 35.6   15.2 / 24.2   19.0 / 17.5
+// (segments aligned to 128 take up to 2 us more by one launch, the same by three).
 constexpr int kOneThreads = 1024, kOneWaves = kOneThreads / kWave, kOneRounds = 8;
 constexpr int64_t kSortOneIds = kOneThreads * kOneRounds, kSortOneRows = 65536;
 template <typename IT, int ROUNDS>
@@ -340,7 +345,8 @@ struct Held {
     if constexpr (VEC == 1) {
       w[0] = __builtin_bit_cast(uint32_t, ld_elem<WD>(p, e));
     } else {
-      const u32x4_t x = ld16<true>((const uint8_t*)p + e * (16 / VEC));  // read once
+      // past the caches: a row is read once, but for grad_out with more than four choices
+      const u32x4_t x = ld16<true>((const uint8_t*)p + e * (16 / VEC));
       w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
     }
   }
@@ -360,7 +366,9 @@ struct Held {
 
 // Four choices' columns are under way at a time; a choice without a row reads
 // row 0 and takes no part.  Rows are read once, past the caches (160 -> 147 us at
-// the sizes above).
+// the sizes above).  Where k is no multiple of four, the loads of row 0 cost: 16384
+// tokens of 2048 bfloat16 columns take 36.0 us with k = 1, 46.3 with 2, 67.6 with 4
+// and 98.9 with 6; two choices at a time 30.7, 37.4, 65.9 and 94.2.
 template <int WD, int VEC, int CH = kLoads<(VEC > 1)>>
 __global__ __launch_bounds__(kThreads) void combine_kernel(ExpertRowArgs a, uint32_t units,
                                                            uint32_t parts) {
@@ -426,7 +434,10 @@ __device__ __forceinline__ float four_sums(const float* d) {
 // WPT waves a token (1, or the 4 of a workgroup) share its columns; four choices
 // at a time.  A choice's gradient is a dot product over the columns: the lanes'
 // parts are added in float32 by exchanges, the waves' in LDS.  (One pass: a
-// choice's row is read for the dot product beside the write of its gradient.)
+// choice's row is read for the dot product beside the write of its gradient.
+// grad_out's row is read again for every four choices: 16384 tokens of 2048
+// bfloat16 columns take 114.6 us with k = 4 and 236.8 with k = 8, of whose traffic
+// the second reading is a seventeenth.)
 template <int WD, int VEC, int WPT>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(ExpertRowArgs a,
                                                                     uint32_t clear_wgs) {

@@ -524,6 +524,16 @@ hipError_t run(const MatmulF8Args& g, hipStream_t s) {
 //   2048 x 1280 (160, 40)    14.2 / 11.9 / 24.4
 //   2048 x 4096 (512, 128)   36.8 / 20.3 / 27.0
 //   4096 x 2560 (640, 160)   45.1 / 31.6 / 26.4
+// The tiles are counted as if all rows were one segment.  With experts the rows of
+// a tile that its segment does not fill are loaded and multiplied all the same, but
+// such products are bound by reading the weights.  4096 columns over 2048, rows an
+// expert (mean), by tile 64 / 128 / 256, the rule's own marked:
+//   16 experts,  32 rows   25.5* / 25.5 / 32.8 us    256 rows   88.9 / 55.0 / 61.8*
+//   64 experts,   2 rows   88.2* / 95.6 / 124.1       64 rows    154 / 126 / 149*
+//   256 experts,  8 rows    409 / 405* / 513          32 rows    493 / 463 / 531*
+//   256 experts, 64 rows    630 / 509 / 552*         256 rows   1545 / 973 / 820*
+// so the 256-row tile, taken for rows that many short segments share, costs up to a
+// fifth there.
 constexpr int64_t kFewTiles = 144;
 template <bool SEG, bool SQ>
 hipError_t by_size(const MatmulF8Args& g, hipStream_t s) {
